@@ -514,10 +514,17 @@ WKV7_API wkv7_status wkv7_gdr_step(int B, int Hk, int Hv, int N, wkv7_dtype x_dt
  *   num_seqs, T_total, cu_seqlens, cu_seqlens_host : as wkv7_prefill
  *   x_dtype       : the type of q, k, v, and the kernel that runs:
  *                   WKV7_BF16 -- the chunked tensor-core kernels (64 tokens a
- *                     chunk; every operand that is not an input is a pair of
- *                     bf16, off by 2^-16 at most, sums are fp32).  A NaN or an
- *                     infinity in a token may spread over the tokens of its own
- *                     chunk and sequence from the chunk's first on;
+ *                     chunk; sums are fp32, an operand that is not an input is
+ *                     a pair of bf16, off by 2^-16 at most, and the inverse that
+ *                     solves a chunk has three terms, 2^-24).  For keys and
+ *                     strengths with 0 <= beta |k|^2 <= 2, where the recurrence
+ *                     does not grow by itself: o and the states are off by about
+ *                     1e-5 of their largest values with keys that differ, 5e-5
+ *                     with keys that repeat and beta = 1, up to 2^-10 with keys
+ *                     that repeat, beta near 2 and hardly any decay.  q, k and v
+ *                     widened to fp32 (exactly) take the other kernel.  A NaN or
+ *                     an infinity in a token may spread over the tokens of its
+ *                     own chunk and sequence from the chunk's first on;
  *                   WKV7_F32 -- a few tokens at a time, fp32 arithmetic throughout;
  *                     how many depends on the sizes and on cu_seqlens_host
  *   q, k          : x_dtype [T_total, Hk, N];  v : x_dtype [T_total, Hv, N]

@@ -18,7 +18,7 @@
 // reverse chain below, keeping G and dv; then one CTA per (chunk, query/key head) for the rest, which
 // sums the value heads that share the head in a fixed order (no atomics: the same inputs give the
 // same bits).
-// Every operand that is not an input is a pair of bf16 (gdr_mma.cuh).
+// Every operand that is not an input is a pair of bf16, That has three terms (gdr_mma.cuh).
 #include "gdr_chain.cuh"
 #include "gdr_internal.cuh"
 #include "gdr_prep.cuh"
@@ -50,9 +50,9 @@ template <int N>
 struct Stage {
     static constexpr uint32_t kKQ = 0;                  // K rows 0-63, Q rows 64-127, [128][64] blocks
     static constexpr uint32_t kO = 2 * C * N * 2;       // dO, [64][64] blocks
-    static constexpr uint32_t kPrep = kO + C * N * 2;   // That, P, d, e
-    static constexpr uint32_t kPrepBytes = 4 * kTile + 2 * C * 4;
-    static constexpr uint32_t kBytes = kPrep + 4 * kTile + 1024;
+    static constexpr uint32_t kPrep = kO + C * N * 2;   // P, That, d, e
+    static constexpr uint32_t kPrepBytes = kGdrPrepVec + 2 * C * 4;
+    static constexpr uint32_t kBytes = kPrep + kGdrPrepVec + 1024;
     static constexpr uint32_t kOutAt = 2 * kBytes;      // dv of one chunk: plain [64][N] bf16, then the low tile
     static constexpr uint32_t kSmem = kOutAt + 2 * C * N * 2;
 };
@@ -112,7 +112,7 @@ __device__ __forceinline__ void reverse_chain(const GdrBackwardArgs &p, const Gd
     };
     // everything below counts steps i = 0 ..; step i is chunk n_chunks - 1 - i
     auto wait_full = [&](int i) { wait(kFull0 + (i & 1), i >> 1); };
-    auto vec_of = [&](int i) { return reinterpret_cast<const float *>(smem + (i & 1) * St::kBytes + St::kPrep + 4 * kTile); };
+    auto vec_of = [&](int i) { return reinterpret_cast<const float *>(smem + (i & 1) * St::kBytes + St::kPrep + kGdrPrepVec); };
 
     if (warp == L::kLoadWarp) {
         if (lane == 0) {
@@ -141,7 +141,7 @@ __device__ __forceinline__ void reverse_chain(const GdrBackwardArgs &p, const Gd
 #pragma unroll 1
         for (int i = 0; i < n_chunks; ++i) {
             const uint32_t s = base + (i & 1) * St::kBytes;
-            const uint32_t kq = s + St::kKQ, ot = s + St::kO, th = s + St::kPrep, ph = th + 2 * kTile;
+            const uint32_t kq = s + St::kKQ, ot = s + St::kO, ph = s + St::kPrep, th = ph + kGdrPrepThat;
             wait_full(i);
             if (i == 0) ptx::named_sync<kTail, L::kWorkers + 32>();  // rows behind the sequence are zeros
             ptx::tc_fence_after_sync();
@@ -174,10 +174,12 @@ __device__ __forceinline__ void reverse_chain(const GdrBackwardArgs &p, const Gd
 #pragma unroll
             for (int ks = 3; ks >= 0; --ks) {  // dv, in x's place
                 const uint32_t id = idesc_bf16(128, 16 * (ks + 1), true);
-                const uint64_t hd = sdesc_across(th + ks * 16 * 128, kTile), ld = sdesc_across(th + kTile + ks * 16 * 128, kTile);
-                mma_bf16(leader, tm + L::kX, tm + L::kPairB + 8 * ks, hd, id, ks < 3);
-                mma_bf16(leader, tm + L::kX, tm + L::kPairB + 32 + 8 * ks, hd, id, 1);
-                mma_bf16(leader, tm + L::kX, tm + L::kPairB + 8 * ks, ld, id, 1);
+                const uint64_t t0 = sdesc_across(th + ks * 16 * 128, kTile), t1 = sdesc_across(th + kTile + ks * 16 * 128, kTile);
+                mma_bf16(leader, tm + L::kX, tm + L::kPairB + 8 * ks, t0, id, ks < 3);
+                mma_bf16(leader, tm + L::kX, tm + L::kPairB + 32 + 8 * ks, t0, id, 1);
+                mma_bf16(leader, tm + L::kX, tm + L::kPairB + 8 * ks, t1, id, 1);
+                mma_bf16(leader, tm + L::kX, tm + L::kPairB + 32 + 8 * ks, t1, id, 1);
+                mma_bf16(leader, tm + L::kX, tm + L::kPairB + 8 * ks, sdesc_across(th + 2 * kTile + ks * 16 * 128, kTile), id, 1);
             }
             commit(leader, bar0 + 8 * kDvDone);
 
@@ -498,7 +500,7 @@ gdr_backward_grad_kernel(const GdrBackwardArgs p, const __grid_constant__ GdrMap
                     ptx::tma_load_2d(at + M::kOv + j * 2 * kTile + kTile, &maps.dv, h * N + j * 64, t0, span);
                 }
                 ptx::bulk_load(base + M::kD, src + gdr_off_dv(N), C * N * 2, span);
-                ptx::bulk_load(base + M::kVec + (r & 1) * 2048, prep + (item0 + r) * kGdrPrepBytes + 4 * kTile, kVecKept * 4, span);
+                ptx::bulk_load(base + M::kVec + (r & 1) * 2048, prep + (item0 + r) * kGdrPrepBytes + kGdrPrepVec, kVecKept * 4, span);
             }
             __syncwarp();
         };

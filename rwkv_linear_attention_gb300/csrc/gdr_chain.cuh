@@ -21,9 +21,10 @@
 //   e err as pairs                         o = Q S0, times scale d
 //   S += K^T (e err)                       err as pairs
 //
-// Precision: K, Q and V are exact bf16; S, r, err, That and P are pairs of bf16 (gdr_mma.cuh),
-// so each product is off by 2^-16 of its operands; sums are fp32 and S itself is never
-// rounded.  One MMA per product instead of two or three would leave 2^-8 in the carried state.
+// Precision: K, Q and V are exact bf16; S, r, err and P are pairs of bf16, That has three terms
+// (gdr_mma.cuh; gdr_prep.cuh says why), so each product is off by 2^-16 of its operands; sums are
+// fp32 and S itself is never rounded.  One MMA per product instead of two or three would leave
+// 2^-8 in the carried state.
 #pragma once
 
 #include "gdr_internal.cuh"
@@ -50,9 +51,9 @@ template <int N>
 struct Stage {
     static constexpr uint32_t kKQ = 0;                  // K rows 0-63, Q rows 64-127, [128][64] blocks
     static constexpr uint32_t kV = 2 * C * N * 2;       // plain [64][N]
-    static constexpr uint32_t kPrep = kV + C * N * 2;   // That, P, d, e
-    static constexpr uint32_t kPrepBytes = 4 * kTile + 2 * C * 4;
-    static constexpr uint32_t kBytes = kPrep + 4 * kTile + 1024;
+    static constexpr uint32_t kPrep = kV + C * N * 2;   // P, That, d, e
+    static constexpr uint32_t kPrepBytes = kGdrPrepVec + 2 * C * 4;
+    static constexpr uint32_t kBytes = kPrep + kGdrPrepVec + 1024;
     static constexpr uint32_t kOutAt = 2 * kBytes;      // o of one chunk, plain [64][N], fp32 or bf16
     static constexpr uint32_t kSmem = kOutAt + C * N * 4;
 };
@@ -182,7 +183,7 @@ __device__ __forceinline__ void chain(const GdrPrefillArgs &p, const GdrMaps &ma
     };
     // chunk c's last MMAs, and so all that they waited for
     auto wait_done = [&](int c) { wait(kDone0 + (c & 1), c >> 1); };
-    auto vec_of = [&](int c) { return reinterpret_cast<const float *>(smem + (c & 1) * St::kBytes + St::kPrep + 4 * kTile); };
+    auto vec_of = [&](int c) { return reinterpret_cast<const float *>(smem + (c & 1) * St::kBytes + St::kPrep + kGdrPrepVec); };
 
     if (warp == L::kLoadWarp) {
         if (lane == 0) {
@@ -191,14 +192,15 @@ __device__ __forceinline__ void chain(const GdrPrefillArgs &p, const GdrMaps &ma
                 if (c >= 2) wait_done(c - 2);  // the stage's chunk is through
                 const uint32_t s = base + (c & 1) * St::kBytes, full = bar0 + 8 * (kFull0 + (c & 1));
                 const int t0 = bos + c * C;
-                ptx::mbar_arrive_expect_tx(full, (kStates ? 2 : 3) * C * N * 2 + St::kPrepBytes);
+                constexpr uint32_t kSkip = kStates ? kGdrPrepThat : 0;  // P is for outputs alone
+                ptx::mbar_arrive_expect_tx(full, (kStates ? 2 : 3) * C * N * 2 + St::kPrepBytes - kSkip);
 #pragma unroll
                 for (int j = 0; j < N / 64; ++j) {
                     ptx::tma_load_2d(s + St::kKQ + j * 2 * kTile, &maps.k, hk * N + j * 64, t0, full);
                     if (!kStates) ptx::tma_load_2d(s + St::kKQ + j * 2 * kTile + kTile, &maps.q, hk * N + j * 64, t0, full);
                 }
                 ptx::tma_load_2d(s + St::kV, &maps.v, h * N, t0, full);
-                ptx::bulk_load(s + St::kPrep, prep + ((slot0 + c) * p.Hv + h) * kGdrPrepBytes, St::kPrepBytes, full);
+                ptx::bulk_load(s + St::kPrep + kSkip, prep + ((slot0 + c) * p.Hv + h) * kGdrPrepBytes + kSkip, St::kPrepBytes - kSkip, full);
             }
         }
         return;
@@ -210,8 +212,9 @@ __device__ __forceinline__ void chain(const GdrPrefillArgs &p, const GdrMaps &ma
 #pragma unroll 1
         for (int c = 0; c < n_chunks; ++c) {
             const uint32_t s = base + (c & 1) * St::kBytes;
-            const uint32_t kq = s + St::kKQ, th = s + St::kPrep, ph = th + 2 * kTile;
-            auto lower = [&](uint32_t d, uint32_t tile, uint32_t first) {  // d (+)= pair B times a lower triangular tile
+            const uint32_t kq = s + St::kKQ, ph = s + St::kPrep, th = ph + kGdrPrepThat;
+            // d (+)= pair B times a lower triangular tile of two or three terms
+            auto lower = [&](uint32_t d, uint32_t tile, int terms, uint32_t first) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {  // tokens 16 ks .. reach columns 16 ks ..
                     const uint32_t id = idesc_bf16(128, 64 - 16 * ks, false);
@@ -219,6 +222,10 @@ __device__ __forceinline__ void chain(const GdrPrefillArgs &p, const GdrMaps &ma
                     mma_bf16(leader, d + 16 * ks, tm + L::kPairB + 8 * ks, ptx::sdesc_sw128(row), id, ks > 0 ? 1u : first);
                     mma_bf16(leader, d + 16 * ks, tm + L::kPairB + 32 + 8 * ks, ptx::sdesc_sw128(row), id, 1);
                     mma_bf16(leader, d + 16 * ks, tm + L::kPairB + 8 * ks, ptx::sdesc_sw128(row + kTile), id, 1);
+                    if (terms == 3) {
+                        mma_bf16(leader, d + 16 * ks, tm + L::kPairB + 32 + 8 * ks, ptx::sdesc_sw128(row + kTile), id, 1);
+                        mma_bf16(leader, d + 16 * ks, tm + L::kPairB + 8 * ks, ptx::sdesc_sw128(row + 2 * kTile), id, 1);
+                    }
                 }
             };
             auto times_state = [&](uint32_t d, uint32_t rows, int half) {  // d (+)= (rows S0)^T, 64 of its columns
@@ -242,7 +249,7 @@ __device__ __forceinline__ void chain(const GdrPrefillArgs &p, const GdrMaps &ma
 
             ptx::named_sync<kResidual, L::kWorkers + 32>();
             ptx::tc_fence_after_sync();
-            lower(tm + L::kX, th, 0);
+            lower(tm + L::kX, th, 3, 0);
             commit(leader, bar0 + 8 * kErrDone);
             if (!kStates) {
                 if (c > 0) ptx::named_sync<kOutRead, L::kOut + 32>();
@@ -269,7 +276,7 @@ __device__ __forceinline__ void chain(const GdrPrefillArgs &p, const GdrMaps &ma
             } else {
                 ptx::named_sync<kOutputs, L::kWorkers + L::kOut + 32>();
                 ptx::tc_fence_after_sync();
-                lower(tm + L::kO, ph, 1);
+                lower(tm + L::kO, ph, 2, 1);
                 commit(leader, bar0 + 8 * (kDone0 + (c & 1)));
             }
         }

@@ -109,10 +109,10 @@ cudaError_t launch_gdr_prefill_scan(const GdrPrefillArgs &args, cudaStream_t str
 inline long long gdr_max_slots(int num_seqs, int T_total) { return static_cast<long long>(T_total) / kGdrChunk + num_seqs; }
 
 // What the chunk kernels share per (slot, value head), written by gdr_prep.cu:
-//   [That hi][That lo][P hi][P lo]  bf16 tiles [64][64] (gdr_mma.cuh)
+//   [P hi][P lo][That in three terms]  bf16 tiles [64][64] (gdr_mma.cuh)
 //   d[64], e[64], beta[64], gam as integer [64] and fraction [64] of log2,
-//   e without beta [64]             fp32
-constexpr int kGdrPrepBytes = 4 * 8192 + 2048;
+//   e without beta [64]                fp32
+constexpr int kGdrPrepThat = 2 * 8192, kGdrPrepVec = 5 * 8192, kGdrPrepBytes = kGdrPrepVec + 2048;
 inline size_t gdr_prep_bytes(int num_seqs, int T_total, int Hv) {
     return static_cast<size_t>(gdr_max_slots(num_seqs, T_total)) * Hv * kGdrPrepBytes;
 }

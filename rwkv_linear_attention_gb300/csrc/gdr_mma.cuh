@@ -9,6 +9,9 @@
 // Pairs.  x = hi + lo with hi = bf16(x), lo = bf16(x - hi): |x - hi - lo| <= 2^-16 |x|.
 // A product of a pair with an exact bf16 operand is two MMAs, of two pairs three (the
 // lo lo term, 2^-16 of the result, is left out).
+//
+// Three terms, the third bf16 of what the pair leaves, hold x to 2^-24 of itself, as fp32
+// does; a product of two such is six MMAs (down to the second order), of one with a pair five.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -126,12 +129,18 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
     sub2(x, y, low(hi), high(hi));
     lo = pack(x, y);
 }
-// The A fragment (16 rows x 16 columns) of an accumulator's two neighbouring column tiles.
-__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-    split(c0[0], c0[1], hi[0], lo[0]);
-    split(c0[2], c0[3], hi[1], lo[1]);
-    split(c1[0], c1[1], hi[2], lo[2]);
-    split(c1[2], c1[3], hi[3], lo[3]);
+// And as three terms.
+__device__ __forceinline__ void split3(float x, float y, uint32_t &a, uint32_t &b, uint32_t &c) {
+    a = pack(x, y);
+    sub2(x, y, low(a), high(a));
+    split(x, y, b, c);
+}
+// The A fragment (16 rows x 16 columns), in three terms, of an accumulator's two neighbouring column tiles.
+__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], uint32_t (&x)[3][4]) {
+    split3(c0[0], c0[1], x[0][0], x[1][0], x[2][0]);
+    split3(c0[2], c0[3], x[0][1], x[1][1], x[2][1]);
+    split3(c1[0], c1[1], x[0][2], x[1][2], x[2][2]);
+    split3(c1[2], c1[3], x[0][3], x[1][3], x[2][3]);
 }
 
 // 16 bytes global -> shared without registers; zeros where `in` is false (src is then not read).

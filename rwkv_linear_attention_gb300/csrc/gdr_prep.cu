@@ -4,12 +4,12 @@
 // One CTA of four warps per (chunk, query/key head): the K and Q rows come by TMA, one MMA forms
 // their products with K in tensor memory (64 columns), and each value head that shares them takes
 // its That and P from those.  The steps of a head are short and follow one another, so latency
-// bounds a CTA and several share an SM; together they are bound by what they write (20 KB of
-// matrices per chunk and head: the blocks above the diagonal are neither written nor read).
+// bounds a CTA and several share an SM; together they are bound by what they write (25 KB of
+// matrices per chunk and head: the blocks above the diagonal are not written; the chains copy whole
+// tiles, but no product of theirs uses those blocks).
 //
-// Measured: 8 x 4096 tokens, 32 heads of 128 in 141 us, 30,000 tokens with 40 heads of 64 in 197 us (43%
-// of the issue slots filled, 3.7 TB/s; warps that wait for one another are most of the rest).  Four CTAs an
-// SM instead of five: 152 us in the first case.
+// Measured: 8 x 4096 tokens, 32 heads of 128 in 177 us, 30,000 tokens with 40 heads of 64 in 230 us.  Four
+// CTAs an SM instead of five: 246 us in the second case.
 #include "gdr_internal.cuh"
 #include "gdr_prep.cuh"
 
@@ -25,12 +25,10 @@ constexpr uint32_t kMaxPolls = 1u << 17;  // of up to 20 us: seconds
 template <int N>
 struct Smem {
     static constexpr uint32_t kRows = 0;                       // K rows 0-63, Q rows 64-127, [128][64] blocks
-    static constexpr uint32_t kThat = 0;                       // in their place: That hi, lo, Ahat hi, lo
-    static constexpr uint32_t kAhat = 2 * kTile;
-    static constexpr uint32_t kDiag = 4 * kTile;
+    static constexpr uint32_t kThat = 0;                       // in their place: That's three tiles
+    static constexpr uint32_t kDiag = 2 * C * N * 2 > 3 * kTile ? 2 * C * N * 2 : 3 * kTile;
     static constexpr uint32_t kVec = kDiag + 4 * 16 * kDiagLd * 4;
     static constexpr uint32_t kBytes = kVec + kHeads * kVecFloats * 4;
-    static_assert(2 * C * N * 2 <= kDiag, "the rows fit where the matrices go");
 };
 
 template <int N>
@@ -109,16 +107,15 @@ gdr_prep_kernel(const GdrPrefillArgs p, const __grid_constant__ GdrMaps maps, un
         }
         float *vec = vecs + w * kVecFloats;
         unsigned char *out = prep + (static_cast<long long>(slot) * p.Hv + hk * rep + r) * kGdrPrepBytes;
-        chunk_matrices<1>(smem, tm, M::kThat, M::kAhat, out + 2 * kTile, reinterpret_cast<float *>(smem + M::kDiag), vec, p.scale, warp,
-                          lane);
+        chunk_matrices<1>(smem, tm, M::kThat, out, reinterpret_cast<float *>(smem + M::kDiag), vec, p.scale, warp, lane);
         if (tid < kVecKept / 4)
-            reinterpret_cast<float4 *>(out + 4 * kTile)[tid] = reinterpret_cast<const float4 *>(vec)[tid];
+            reinterpret_cast<float4 *>(out + kGdrPrepVec)[tid] = reinterpret_cast<const float4 *>(vec)[tid];
         __syncthreads();
 #pragma unroll 4
-        for (int i = tid; i < 2 * C * 8; i += kThreads) {  // That's blocks on and below the diagonal
+        for (int i = tid; i < 3 * C * 8; i += kThreads) {  // That's blocks on and below the diagonal
             const int row = (i >> 3) & (C - 1);
             if ((((i & 7) ^ (row & 7)) >> 1) <= (row >> 4))
-                *reinterpret_cast<uint4 *>(out + i * 16) = *reinterpret_cast<const uint4 *>(smem + M::kThat + i * 16);
+                *reinterpret_cast<uint4 *>(out + kGdrPrepThat + i * 16) = *reinterpret_cast<const uint4 *>(smem + M::kThat + i * 16);
         }
     }
     ptx::tc_fence_before_sync();

@@ -22,8 +22,14 @@
 // blocks in fp32, one column per lane by substitution (stable for any Ahat, unlike its powers),
 // while the other two form P.  Then warp j forms the blocks below diagonal block j,
 // T_ij = -T_ii sum_{j <= m < i} A_im T_mj, transposed on the tensor cores: T_mj^T is a left
-// operand in registers, A_im^T and T_ii^T are right operands read from pairs of bf16 tiles
+// operand in registers, A_im^T and T_ii^T are right operands read from bf16 tiles
 // (gdr_mma.cuh), and no warp waits for another between the blocks of its column.
+//
+// That and the products that form it are in three bf16 terms, where pairs serve for the rest: with keys that
+// repeat and strengths near 2, That's elements stay near 2 all over the chunk and That times a
+// vector is a small difference of large terms.  With That in pairs, 1024 tokens of one key of 128 channels
+// with strength 2 and no decay came out 3e-2 off; in three terms, 5e-4 (independent keys: 7e-6
+// either way).
 #pragma once
 
 #include "gdr_internal.cuh"
@@ -110,14 +116,15 @@ __device__ __forceinline__ float keep(bool c, float x) {
 
 constexpr int kDiagLd = 20;  // fp32 row stride of a diagonal block
 
-// Four warps (w = 0 .. 3, the TMEM lane quarter each): That and P of a chunk as pairs from the
-// products at TMEM column `gram`: That hi, lo into shared memory at `t_at`, P hi, lo straight to `p_out`.
-// `ahat_at`: two tiles of scratch, `diag`: four blocks of 16 x kDiagLd floats; BAR: a named
-// barrier of these four warps, which they have passed since any of the scratch was read.
+// Four warps (w = 0 .. 3, the TMEM lane quarter each): That and P of a chunk from the products at TMEM
+// column `gram`: That's three tiles into shared memory at `t_at`, P hi, lo straight to `p_out`.
+// Ahat's block (i, m), i > m, lies meanwhile in That's place for (m, i), which is not That's own.
+// `diag`: four blocks of 16 x kDiagLd floats; BAR: a named barrier of these four warps, which they
+// have passed since any of the scratch was read.
 template <int BAR>
-__device__ __forceinline__ void chunk_matrices(unsigned char *smem, uint32_t gram, uint32_t t_at, uint32_t ahat_at,
-                                               unsigned char *p_out, float *diag, const float *vec, float scale, int w, int lane) {
-    const uint32_t base = ptx::smem_addr(smem), ttile = base + t_at, atile = base + ahat_at;
+__device__ __forceinline__ void chunk_matrices(unsigned char *smem, uint32_t gram, uint32_t t_at, unsigned char *p_out, float *diag,
+                                               const float *vec, float scale, int w, int lane) {
+    const uint32_t ttile = ptx::smem_addr(smem) + t_at;
     {
         const int t = (w & 1) * 32 + lane, own = t >> 4;  // this thread's row and its block row
         const bool is_q = w >= 2;
@@ -127,7 +134,7 @@ __device__ __forceinline__ void chunk_matrices(unsigned char *smem, uint32_t gra
         const float *colf = vec + kVecCol + (own > 0 ? own - 1 : 0) * 48;
         float y[16];
 #pragma unroll 1
-        for (int p = 0; p < parts; ++p) {  // the blocks left of the diagonal, as pairs
+        for (int p = 0; p < parts; ++p) {  // the blocks left of the diagonal
             float x[16];
             tm_ld<16>(gram + (static_cast<uint32_t>(w * 32) << 16) + p * 16, x);
 #pragma unroll
@@ -141,10 +148,23 @@ __device__ __forceinline__ void chunk_matrices(unsigned char *smem, uint32_t gra
                     mul2(x[i], x[i + 1], row);
                     mul2(x[i + 2], x[i + 3], row);
                 }
-                uint32_t hi[8], lo[8];
-                split_row<16>(x, hi, lo);
-                if (is_q) store_row_global<C>(p_out, p_out + kTile, t, p * 16, hi, lo);
-                else store_row<C>(smem + ahat_at, smem + ahat_at + kTile, t, p * 16, hi, lo);
+                if (is_q) {
+                    uint32_t hi[8], lo[8];
+                    split_row<16>(x, hi, lo);
+                    store_row_global<C>(p_out, p_out + kTile, t, p * 16, hi, lo);
+                } else {
+                    uint32_t x0[8], x1[8], x2[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split3(x[2 * i], x[2 * i + 1], x0[i], x1[i], x2[i]);
+                    unsigned char *at = smem + t_at;
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        const uint32_t off = tile_off<C>(p * 16 + (t & 15), own * 16 + 2 * i);
+                        *reinterpret_cast<uint4 *>(at + off) = make_uint4(x0[i], x0[i + 1], x0[i + 2], x0[i + 3]);
+                        *reinterpret_cast<uint4 *>(at + off + kTile) = make_uint4(x1[i], x1[i + 1], x1[i + 2], x1[i + 3]);
+                        *reinterpret_cast<uint4 *>(at + off + 2 * kTile) = make_uint4(x2[i], x2[i + 1], x2[i + 2], x2[i + 3]);
+                    }
+                }
             }
         }
         const int last = is_q ? t & 15 : (t & 15) - 1;  // the last column of the diagonal block that counts
@@ -192,57 +212,54 @@ __device__ __forceinline__ void chunk_matrices(unsigned char *smem, uint32_t gra
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
+            const __nv_bfloat16 x0 = __float2bfloat16_rn(x[i]);
+            const float left = x[i] - __bfloat162float(x0);
+            const __nv_bfloat16 x1 = __float2bfloat16_rn(left);
             const uint32_t off = t_at + tile_off<C>(blk * 16 + i, blk * 16 + j) + (j & 7) * 2;
-            *reinterpret_cast<__nv_bfloat16 *>(smem + off) = hi;
-            *reinterpret_cast<__nv_bfloat16 *>(smem + off + kTile) = __float2bfloat16_rn(x[i] - __bfloat162float(hi));
+            *reinterpret_cast<__nv_bfloat16 *>(smem + off) = x0;
+            *reinterpret_cast<__nv_bfloat16 *>(smem + off + kTile) = x1;
+            *reinterpret_cast<__nv_bfloat16 *>(smem + off + 2 * kTile) = __float2bfloat16_rn(left - __bfloat162float(x1));
         }
     }
     ptx::named_sync<BAR, 128>();
     // the blocks below the diagonal: T_mj^T for j = w as left operands
     if (w == 3) return;
-    uint32_t th[4][4], tl[4][4];
+    uint32_t t[4][3][4];  // by block row, in three terms
 #pragma unroll
     for (int m = 0; m < 3; ++m)
-        if (m == w) {
-            load_at<C>(ttile, m * 16, m * 16, lane, th[m]);
-            load_at<C>(ttile + kTile, m * 16, m * 16, lane, tl[m]);
+        if (m == w)
+#pragma unroll
+            for (int x = 0; x < 3; ++x) load_at<C>(ttile + x * kTile, m * 16, m * 16, lane, t[m][x]);
+    // d += a times the block at (row, col): the products of terms down to the second order, the smallest first
+    auto times = [&](float (&d)[2][4], const uint32_t (&a)[3][4], int row, int col) {
+#pragma unroll
+        for (int y = 2; y >= 0; --y) {
+            uint32_t b[4];
+            load_b<C>(ttile + y * kTile, row, col, lane, b);
+#pragma unroll
+            for (int x = 2 - y; x >= 0; --x)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) mma(d[c], a[x], b[2 * c], b[2 * c + 1]);
         }
+    };
 #pragma unroll
     for (int i = 1; i < 4; ++i) {
         if (i <= w) continue;
         float acc[2][4] = {}, res[2][4] = {};
 #pragma unroll
-        for (int m = 0; m < i; ++m) {
-            if (m < w) continue;
-            uint32_t bh[4], bl[4];
-            load_b<C>(atile, i * 16, m * 16, lane, bh);
-            load_b<C>(atile + kTile, i * 16, m * 16, lane, bl);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                mma(acc[c], th[m], bh[2 * c], bh[2 * c + 1]);
-                mma(acc[c], tl[m], bh[2 * c], bh[2 * c + 1]);
-                mma(acc[c], th[m], bl[2 * c], bl[2 * c + 1]);
-            }
-        }
+        for (int m = 0; m < i; ++m)
+            if (m >= w) times(acc, t[m], m * 16, i * 16);  // Ahat_im, in the place for (m, i)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[c][e] = -acc[c][e];
-        uint32_t hi[4], lo[4], bh[4], bl[4];
-        split_a(acc[0], acc[1], hi, lo);
-        load_b<C>(ttile, i * 16, i * 16, lane, bh);
-        load_b<C>(ttile + kTile, i * 16, i * 16, lane, bl);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            mma(res[c], hi, bh[2 * c], bh[2 * c + 1]);
-            mma(res[c], lo, bh[2 * c], bh[2 * c + 1]);
-            mma(res[c], hi, bl[2 * c], bl[2 * c + 1]);
-        }
-        split_a(res[0], res[1], th[i], tl[i]);
+        uint32_t a[3][4];
+        split_a(acc[0], acc[1], a);
+        times(res, a, i * 16, i * 16);
+        split_a(res[0], res[1], t[i]);
         const uint32_t at = tile_off<C>(i * 16 + ((lane >> 4) << 3) + (lane & 7), w * 16 + (lane & 8));
-        stsm4t(ttile + at, th[i][0], th[i][1], th[i][2], th[i][3]);
-        stsm4t(ttile + kTile + at, tl[i][0], tl[i][1], tl[i][2], tl[i][3]);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) stsm4t(ttile + x * kTile + at, t[i][x][0], t[i][x][1], t[i][x][2], t[i][x][3]);
     }
 }
 
