@@ -215,8 +215,8 @@ WKV7_API wkv7_status wkv7_verify_commit(int B, int T, int H, int N, const float 
  *
  * With uniform u the kept tokens and next_token are distributed as samples of
  * the target alone.  When m is zero everywhere, p_n itself is sampled; when
- * that has no weight either, or an infinite one, next_token is -1.  A NaN
- * weighs nothing.  The comparisons hold 48 bits and the running sums at least
+ * that has no weight either, an infinite one, or a sum beyond fp32, next_token
+ * is -1.  A NaN weighs nothing.  The comparisons hold 48 bits and the running sums at least
  * 44, in a fixed order: the same inputs always give the same answer.
  *
  *   K             : drafts per row, 1 .. WKV7_ACCEPT_MAX_DRAFTS

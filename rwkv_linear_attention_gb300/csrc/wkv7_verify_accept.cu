@@ -56,6 +56,7 @@ __device__ __forceinline__ Pair scale(float u, Pair a) {  // u a
     const float hi = __fadd_rn(p, e);
     return {hi, __fsub_rn(e, __fsub_rn(hi, p))};
 }
+__device__ __forceinline__ Pair times_power(Pair a, float p) { return {a.hi * p, a.lo * p}; }  // p a power of two: exact
 __device__ __forceinline__ Pair shfl_xor(Pair a, int m) {
     return {__shfl_xor_sync(0xffffffffu, a.hi, m), __shfl_xor_sync(0xffffffffu, a.lo, m)};
 }
@@ -197,8 +198,14 @@ wkv7_verify_accept_kernel(const AcceptArgs a, int segs_per_cta) {
             if (r == rank) upto = total;
         }
         if (total.hi > 0.f && total.hi < INFINITY) {
-            const Pair thr = scale(u, total);
-            if (warp == 0 && !less(thr, before) && less(thr, upto)) {
+            // The threshold and what is compared with it are taken 2^64 times as large where that
+            // leaves room: near the smallest fp32 numbers u times the total would round to the
+            // total itself, and no sum would pass it.  So enlarged, u total < total holds, and the
+            // ranges [before, upto) of the row's CTAs leave no gap: one of them has the threshold.
+            const float up = total.hi < 0x1p60f ? 0x1p64f : 1.f;
+            const Pair thr = scale(u, times_power(total, up));
+            auto past_at = [&](Pair sum) { return less(thr, times_power(sum, up)); };
+            if (warp == 0 && !past_at(before) && past_at(upto)) {
                 // the first segment whose running sum passes the threshold (rounding may leave
                 // it past the last one: then the last with any weight)
                 Pair at = before, seg_at = before;
@@ -209,7 +216,7 @@ wkv7_verify_accept_kernel(const AcceptArgs a, int segs_per_cta) {
                     const Pair incl = add(at, warp_scan(own, lane));
                     Pair excl{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
                     if (lane == 0) excl = at;
-                    const unsigned past = __ballot_sync(0xffffffffu, own.hi > 0.f && less(thr, incl));
+                    const unsigned past = __ballot_sync(0xffffffffu, own.hi > 0.f && past_at(incl));
                     const unsigned any = __ballot_sync(0xffffffffu, own.hi > 0.f);
                     const int pick = past ? __ffs(past) - 1 : any ? 31 - __clz(any) : 0;
                     const Pair pick_at{__shfl_sync(0xffffffffu, excl.hi, pick), __shfl_sync(0xffffffffu, excl.lo, pick)};
@@ -244,7 +251,7 @@ wkv7_verify_accept_kernel(const AcceptArgs a, int segs_per_cta) {
                     c = add(c, w[j]);
                     if (w[j].hi > 0.f) {
                         pos = v0 + j;
-                        if (hit < 0 && less(thr, c)) hit = v0 + j;
+                        if (hit < 0 && past_at(c)) hit = v0 + j;
                     }
                 }
                 const unsigned hits = __ballot_sync(0xffffffffu, hit >= 0), poss = __ballot_sync(0xffffffffu, pos >= 0);
