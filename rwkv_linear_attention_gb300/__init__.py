@@ -486,58 +486,6 @@ def verify_accept(draft_tokens, target_probs, u_accept, u_sample, draft_probs=No
     return accept_len, next_token
 
 
-def _host_seqlens(cu_seqlens_host, n):
-    if cu_seqlens_host is None:
-        return None
-    if cu_seqlens_host.device.type != "cpu" or cu_seqlens_host.dtype != torch.int32:
-        raise TypeError("cu_seqlens_host must be a CPU int32 tensor")
-    if tuple(cu_seqlens_host.shape) != (n,):
-        raise ValueError(f"cu_seqlens_host has shape {tuple(cu_seqlens_host.shape)}, expected {(n,)}")
-    return cu_seqlens_host.contiguous()
-
-
-def verify_accept(draft_tokens, target_probs, u_accept, u_sample, draft_probs=None, draft_lens=None,
-                  accept_len=None, next_token=None, stream=None):
-    """Which drafted tokens a verify pass keeps, and the token after them.
-
-    ``draft_tokens`` int32 [B, K]; ``target_probs`` fp32 [B, K + 1, V], the target's
-    distribution at each position of the verify pass; ``draft_probs`` fp32
-    [B, K, V], what the drafts were sampled from (None: they are taken as certain);
-    ``u_accept`` [B, K] and ``u_sample`` [B], fp32 uniforms in [0, 1);
-    ``draft_lens`` int32 [B], the drafts each row has (None: all K).
-
-    Draft i is kept while ``u_accept * q_i(x_i) < p_i(x_i)``; the next token is drawn
-    by ``u_sample`` from max(p - q, 0) at the first refusal, or from the last
-    distribution.  Returns ``(accept_len, next_token)``, int32 [B] each:
-    ``accept_len`` counts the row's own token and its kept drafts, which is what
-    :func:`verify_commit` takes; ``next_token`` is -1 where there is no weight."""
-    _need_cuda("draft_tokens", draft_tokens, torch.int32)
-    B, K = draft_tokens.shape
-    V = target_probs.shape[-1]
-    dev = draft_tokens.device
-    lib = _lib._lib or _lib.load()
-    args = (("target_probs", target_probs, torch.float32, (B, K + 1, V)),
-            ("u_accept", u_accept, torch.float32, (B, K)), ("u_sample", u_sample, torch.float32, (B,)),
-            ("draft_probs", draft_probs, torch.float32, (B, K, V)), ("draft_lens", draft_lens, torch.int32, (B,)))
-    with _on(dev, stream):
-        if accept_len is None:
-            accept_len = torch.empty(B, device=dev, dtype=torch.int32)
-        if next_token is None:
-            next_token = torch.empty(B, device=dev, dtype=torch.int32)
-        for name, t, dtype, shape in (*args, ("accept_len", accept_len, torch.int32, (B,)),
-                                      ("next_token", next_token, torch.int32, (B,))):
-            if t is not None and not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
-                _need_cuda(name, t, dtype, shape)
-                _same_device(dev, t)
-        st = lib.wkv7_verify_accept(B, K, V, draft_tokens.data_ptr(), None if draft_lens is None else draft_lens.data_ptr(),
-                                    target_probs.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
-                                    u_accept.data_ptr(), u_sample.data_ptr(), accept_len.data_ptr(), next_token.data_ptr(),
-                                    _stream_handle(stream, dev))
-    if st:
-        _lib.check(st, "wkv7_verify_accept")
-    return accept_len, next_token
-
-
 def _gdr_inputs(q, k, v, g, beta, lead):
     """Checks of the gated delta rule's inputs, ``lead`` their leading size; returns (Hk, Hv, N).
     One cheap pass; inputs that fail it are checked again one by one for a precise error."""
