@@ -200,6 +200,8 @@ __device__ __forceinline__ void reverse_chain(const GdrBackwardArgs &p, const Gd
             }
             commit(leader, bar0 + 8 * (kDone0 + (i & 1)));
         }
+        // nobody else waits for the last chunks': their arrivals must not find another CTA's memory
+        for (int i = max(n_chunks - 2, 0); i < n_chunks; ++i) wait(kDone0 + (i & 1), i >> 1);
         ptx::named_sync<kLast, L::kWorkers + L::kOut + 32>();  // the last of it has been read
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tm, 512);

@@ -280,6 +280,8 @@ __device__ __forceinline__ void chain(const GdrPrefillArgs &p, const GdrMaps &ma
                 commit(leader, bar0 + 8 * (kDone0 + (c & 1)));
             }
         }
+        if (kStates)  // nobody else waits for the last chunks': their arrivals must not find another CTA's memory
+            for (int c = max(n_chunks - 2, 0); c < n_chunks; ++c) wait_done(c);
         ptx::named_sync<kLast, L::kWorkers + kOuts + 32>();  // the last of it has been read
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tm, 512);
