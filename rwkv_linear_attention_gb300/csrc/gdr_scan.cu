@@ -18,10 +18,9 @@
 // memory, filled by asynchronous copies; the products for the next kTok tokens are formed while
 // these are worked on, by four more warps (the feeders) or by the same.  Tokens behind a
 // sequence's last are filled with zeros.
-#include <algorithm>
-
 #include "gdr_internal.cuh"
 #include "gdr_mma.cuh"
+#include "gdr_split.h"
 #include "sm103_ptx.cuh"
 
 namespace wkv7 {
@@ -335,45 +334,10 @@ cudaError_t run(const GdrPrefillArgs &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// Which split.  A warp of 8 columns takes 0.72 of the time per token of one of 16, but a head then
-// has twice the CTAs; with feeders a CTA takes an SM's registers, and without them several
-// share one, which costs each less than waiting its turn.  In units of a token of 16 columns with
-// feeders (0.17 us at N = 64, 0.24 at 128), the time until the busiest of 152 SMs is done.
-// Measured, in us (8 columns, 16 with feeders, 16 without), 1000 tokens a sequence:
-//   40 heads of 64,  1 sequence 121 172 191   2 sequences 233 171 189   4 sequences 343 332 283   16 sequences 1019 821 644
-//   32 heads of 128, 1 sequence 182 244 264   2 sequences 356 245 264   4 sequences 704 476 437   16 sequences 2448 1650 1456
-// and 500, 1000 and 37 tokens with 40 heads of 64: 124 173 192.
-enum Split { kNarrow, kWide, kShared };
-Split choose(const GdrPrefillArgs &p) {
-    constexpr int kSms = 152, kSorted = 32;
-    double lens[kSorted], total = p.T_total, longest = total / p.num_seqs;  // lens: longest first
-    const int n = p.num_seqs <= kSorted ? p.num_seqs : 0;
-    for (int i = 0; i < p.num_seqs; ++i) {
-        const double len = p.cu_seqlens_host ? p.cu_seqlens_host[i + 1] - p.cu_seqlens_host[i] : total / p.num_seqs;
-        longest = std::max(longest, len);
-        if (n == 0) {
-            if (!p.cu_seqlens_host) break;
-            continue;
-        }
-        int at = i;
-        for (; at > 0 && lens[at - 1] < len; --at) lens[at] = lens[at - 1];
-        lens[at] = len;
-    }
-    auto busiest = [&](long long ctas) {  // of each sequence; no SM can be done before
-        double most = std::max(longest, total * ctas / kSms);
-        for (long long turn = 1; turn * kSms / ctas < n; ++turn) most = std::max(most, (turn + 1) * lens[turn * kSms / ctas]);
-        return most;
-    };
-    const double wide = busiest(static_cast<long long>(p.Hv) * (p.N / 64)), narrow = 0.72 * busiest(static_cast<long long>(p.Hv) * (p.N / 32));
-    const double shared = 0.3 * longest + 0.75 * wide;
-    if (static_cast<long long>(p.num_seqs) * p.Hv * (p.N / 32) > (1 << 24)) return kShared;  // far from the grid's limit
-    return narrow <= std::min(wide, shared) ? kNarrow : wide <= shared ? kWide : kShared;
-}
-
 template <int N>
 cudaError_t prefill(const GdrPrefillArgs &p, cudaStream_t stream) {
-    const Split s = choose(p);
-    return s == kNarrow ? run<N, 2, true>(p, stream) : s == kWide ? run<N, 4, true>(p, stream) : run<N, 4, false>(p, stream);
+    const GdrSplit s = gdr_choose_split(p.num_seqs, p.T_total, p.Hv, N, p.cu_seqlens_host);
+    return s == kGdrNarrow ? run<N, 2, true>(p, stream) : s == kGdrWide ? run<N, 4, true>(p, stream) : run<N, 4, false>(p, stream);
 }
 
 }  // namespace
