@@ -41,8 +41,9 @@ using namespace gdr;
 //   -d dv as pairs                         dv out, and kept as pairs
 //   G += Q^T (scale d dO) + K^T (-d dv), the first 64 of its columns before the second
 //
-// What the chains keep (96 KB each per chunk and head of 128) is half of what they move, and that
-// bounds them: 453 us together at 4 x 4096 tokens and 32 heads of 128, 5.8 TB/s.
+// What the chains keep (96 KB each per chunk and head of 128) is more than half of what they move, and
+// that bounds them: 466 us together at 4 x 4096 tokens and 32 heads of 128, in which 2.6 GB go through
+// HBM (5.5 TB/s).
 
 constexpr uint32_t kMaxPolls = 1u << 17;  // of up to 20 us: seconds
 
@@ -390,7 +391,7 @@ __device__ __forceinline__ void reverse_chain(const GdrBackwardArgs &p, const Gd
 
 // Both chains of every (sequence, value head), which need nothing from one another: the reverse ones
 // first, as they take longer.  One after the other, six documents to 300 tokens took 66 us a call
-// instead of 45; where HBM bounds them, the same.
+// instead of 45 (47 now); where HBM bounds them, the same.
 template <int N>
 __global__ void __launch_bounds__(Chain<N>::kWarps * 32)
 gdr_backward_chains_kernel(const GdrBackwardArgs p, const __grid_constant__ GdrMaps maps, const unsigned char *__restrict__ prep,
@@ -411,7 +412,7 @@ gdr_backward_chains_kernel(const GdrBackwardArgs p, const __grid_constant__ GdrM
 //
 // Sixteen warps hold dq and dk in registers over the heads that share them, four threads a row,
 // and take each product out of tensor memory once (with eight, half of the issue slots stayed
-// empty: 494 us where this takes 437); one issues the MMAs and the copies, and one sums a
+// empty: 494 us where this took 437, and takes 443); one issues the MMAs and the copies, and one sums a
 // head's dbeta and dg while the others go on to the next.  S0 and G (128 KB as pairs) do not fit
 // beside the rest at once with the next head's: of two places one has S0, and the other err, dO
 // and dv until those are in tensor memory, then G.  The next head has them the other way round,

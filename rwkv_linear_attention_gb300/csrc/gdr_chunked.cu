@@ -1,12 +1,12 @@
 // Chunked prefill of the gated delta rule (wkv7_gdr_prefill with bf16 inputs): the chains of
 // gdr_chain.cuh, over whole sequences or segments of them.
 //
-// Measured: 8 x 4096 tokens, 32 heads of 128, in 269 us (256 chains, 152 at a time, 64 chunks of
-// 2.1 us: the three products on the chain are 0.8 of it, the hand-overs between threads and MMAs
-// the rest); 30,000 tokens in ten sequences, 40 heads of 64, in 234 us.  Before, with the state in
-// the registers of warps that issue mma.sync, the first took 776 us; with the chunk's matrices formed
-// inside the chain's CTA, 600 us for both where this and gdr_prep.cu take 410 (the code no longer
-// fits the instruction cache).
+// Measured: 8 x 4096 tokens, 32 heads of 128, in 293 us (256 chains, 152 at a time, 64 chunks of
+// 2.3 us: the three products on the chain are 0.9 of it, the hand-overs between threads and MMAs
+// the rest; with That in two terms instead of three 269 us); 30,000 tokens in ten sequences, 40 heads of
+// 64, in 250 us.  Before, with the state in the registers of warps that issue mma.sync, the first took 776
+// us; with the chunk's matrices formed inside the chain's CTA, 600 us for both where this and
+// gdr_prep.cu then took 410 (the code no longer fits the instruction cache).
 #include <algorithm>
 
 #include "gdr_chain.cuh"
@@ -122,13 +122,13 @@ gdr_segment_chain_kernel(const Segments seg, const void *initial_state, wkv7_dty
 constexpr int kSms = 152;
 
 // Segments per sequence.  With n chunks a sequence and both passes' chains on the SMs at once, a
-// segmented call takes n / count chunk steps twice (1.7 us without outputs, 2.1 with them) instead
+// segmented call takes n / count chunk steps twice (1.75 us without outputs, 2.3 with them) instead
 // of n once, and about 15 us for the small kernel and two more launches: 48 chunks in 8 segments
 // take 22 + 15 us instead of 86, 24 in 3 take 29 + 15 instead of 43.  If one segment more would
 // leave few of the first pass's runs without an SM, the two runs of the last segment that it runs
 // are made half as long, come last, and share: 32768 tokens with 32 heads of 128 in 732 us
-// instead of 805 in three equal segments (700 since then).  The sequences' mean length decides, which
-// host and device know alike.
+// instead of 805 in three equal segments (both measured when a step took 1.7 and 2.1).  The sequences'
+// mean length decides, which host and device know alike: one long sequence among short ones is not cut.
 Segments segments(int num_seqs, int T_total, int Hv) {
     const long long pairs = static_cast<long long>(num_seqs) * Hv;
     if (pairs == 0) return {1, false, nullptr};

@@ -39,7 +39,8 @@ inline cudaError_t gdr_allow_smem(const void *kernel, int bytes, std::atomic<uns
 // any launch.  A kernel lets the next one come only once its own tensor memory is allocated (a later
 // allocation could stand in its way), and the chains that run for states alone not before they end:
 // the small kernel behind them would crowd the SMs that are free first.  The backward of six documents
-// to 300 tokens took 75 us without and 67 with, prefill of 32768 tokens 726 and 719.
+// to 300 tokens took 75 us without and 67 with, prefill of 32768 tokens 726 and 719 (measured when the
+// backward's chains still were two launches).
 template <typename... Params, typename... Args>
 inline cudaError_t gdr_launch(void (*kernel)(Params...), dim3 grid, unsigned threads, int smem, cudaStream_t stream, bool behind,
                               const Args &...args) {
